@@ -199,7 +199,7 @@ def _plain_xent(s, case):
     count = valid.sum()
     mean = token.sum() / count.clamp(min=1)
     if not case["train"]:
-        return mean, token, torch.where(valid, lse[:, 0], torch.zeros_like(token))
+        return mean, token, lse[:, 0]
     p = torch.exp(z - lse)
     p = p.scatter_add(1, index, torch.full_like(index, -1, dtype=p.dtype))
     p = p * (valid.float() * s["dloss"] / count.clamp(min=1))[:, None]
@@ -333,7 +333,7 @@ def exact(case, seed):
             token = F.cross_entropy(z, s["target"], ignore_index=IGNORE, reduction="none")
             mean = token.sum() / max(1, int((s["target"] != IGNORE).sum()))
             if not train:
-                return mean, token, torch.logsumexp(z, dim=1) * (s["target"] != IGNORE)
+                return mean, token, torch.logsumexp(z, dim=1)
             return (mean.detach(), token.detach(),
                     *torch.autograd.grad(mean, leaves, s["dloss"].double()))
         q, k, wq, wk = leaves = [leaf(n) for n in ("q", "k", "q_weight", "k_weight")]
