@@ -263,6 +263,14 @@ def _own(s, case):
                                            activation=case["act"]))
     if case["op"] == "linear_xent":
         a = s["x"], s["weight"], s["target"]
+        if not case["train"] and case["ignored"]:
+            # every token's log-sum-exp is asked for, where the operator leaves out the
+            # tokens without a loss: all are scored, these left out of the loss afterwards
+            valid = s["target"] != IGNORE
+            _, token, lse = ops.linear_cross_entropy_forward(
+                s["x"], s["weight"], s["target"].clamp(min=0), "none", IGNORE)
+            token = torch.where(valid, token, torch.zeros_like(token))
+            return token.sum() / valid.sum().clamp(min=1), token, lse
         mean, token, lse = ops.linear_cross_entropy_forward(*a, ignore_index=IGNORE)
         if not case["train"]:
             return mean, token, lse
