@@ -456,12 +456,13 @@ int apexw_destroy(apexw_t h);
  * APEXW_BF16).  Matrix operands are row major; base pointers are 16-byte
  * aligned (APEXW_EINVAL otherwise).  Sums, softmax statistics and norms are
  * fp32; every output is rounded once.  They keep the rules above: the caller
- * owns all device memory and the stream, nothing is allocated, nothing
- * synchronises, arguments are checked before anything is queued, and the same
- * inputs give the same bits (no atomics).  Workspaces and kept buffers are
- * 256-byte aligned; a workspace may be reused by the next call on the same
- * stream.  All calls may be captured into a graph.  Any of a gradient's output
- * pointers may be NULL: then that gradient is not computed.
+ * owns all device memory and the stream, whose device is the calling thread's
+ * current one; nothing is allocated, nothing synchronises, arguments are checked
+ * before anything is queued, and the same inputs give the same bits (no
+ * atomics).  Workspaces and kept buffers are 256-byte aligned; a workspace may be
+ * reused by the next call on the same stream.  All calls may be captured into a
+ * graph.  Any of a gradient's output pointers may be NULL: then that gradient is
+ * not computed.
  */
 
 /* ---- gated feed-forward block

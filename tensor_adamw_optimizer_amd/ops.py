@@ -32,6 +32,20 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _queue(call, device: torch.device, *args) -> None:
+    """The library's call on torch's current stream of the tensors' device, that
+    device made current: a raw stream, and the default one, 0, above all, is one of
+    the thread's current device."""
+    if _current_device() == device.index:
+        call(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            call(*args, _stream(device))
+
+
 def _sig(t: torch.Tensor):
     return t.shape, t.stride(), t.dtype, t.device
 
@@ -151,9 +165,9 @@ def gated_ffn_forward(x, w_gate, w_up, w_down, activation: str = "silu", keep: b
     y = _empty(x)
     kept = _empty(kept_like) if keep else None
     ws = _empty(ws_like)
-    L.apexw_gated_ffn_forward(s, xr.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-                              w_down.data_ptr(), y.data_ptr(), kept.data_ptr() if keep else 0,
-                              kept_len, ws.data_ptr(), n, _stream(x.device))
+    _queue(L.apexw_gated_ffn_forward, x.device, s, xr.data_ptr(), w_gate.data_ptr(),
+           w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(), kept.data_ptr() if keep else 0,
+           kept_len, ws.data_ptr(), n)
     return y, kept
 
 
@@ -170,12 +184,10 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, kept: Optional[torch.Tensor]
     xr, dyr = x if direct else _copy(x), dy if dy_direct else _copy(dy)
     outs = [_empty(t) if need else None for t, need in zip((x, w_gate, w_up, w_down), needs)]
     ws = _empty(ws_like)
-    L.apexw_gated_ffn_backward(s, dyr.data_ptr(), xr.data_ptr(), w_gate.data_ptr(),
-                               w_up.data_ptr(), w_down.data_ptr(),
-                               0 if kept is None else kept.data_ptr(),
-                               0 if kept is None else kept.numel(),
-                               *(0 if o is None else o.data_ptr() for o in outs),
-                               ws.data_ptr(), n, _stream(x.device))
+    _queue(L.apexw_gated_ffn_backward, x.device, s, dyr.data_ptr(), xr.data_ptr(),
+           w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+           0 if kept is None else kept.data_ptr(), 0 if kept is None else kept.numel(),
+           *(0 if o is None else o.data_ptr() for o in outs), ws.data_ptr(), n)
     return tuple(outs)
 
 
@@ -237,9 +249,9 @@ def linear_cross_entropy_forward(x, weight, target, reduction: str = "mean",
     xr, w, tg = x if direct else _copy(x), _whole(weight), target.contiguous()
     loss = None if reduction == "none" else _empty(loss_like)
     token, lse, ws = _empty(token_like), _empty(token_like), _empty(ws_like)
-    L.apexw_linear_xent_forward(s, xr.data_ptr(), w.data_ptr(), tg.data_ptr(),
-                                0 if loss is None else loss.data_ptr(), token.data_ptr(),
-                                lse.data_ptr(), ws.data_ptr(), n, _stream(x.device))
+    _queue(L.apexw_linear_xent_forward, x.device, s, xr.data_ptr(), w.data_ptr(), tg.data_ptr(),
+           0 if loss is None else loss.data_ptr(), token.data_ptr(), lse.data_ptr(),
+           ws.data_ptr(), n)
     return loss, token, lse
 
 
@@ -261,9 +273,9 @@ def linear_cross_entropy_backward(x, weight, target, lse, dloss, reduction: str 
     lse, dloss = lse.contiguous(), dloss.contiguous()
     outs = [_empty(t) if need else None for t, need in zip((x, weight), needs)]
     ws = _empty(ws_like)
-    L.apexw_linear_xent_backward(s, dloss.data_ptr(), xr.data_ptr(), w.data_ptr(), tg.data_ptr(),
-                                 lse.data_ptr(), *(0 if o is None else o.data_ptr() for o in outs),
-                                 ws.data_ptr(), n, _stream(dev))
+    _queue(L.apexw_linear_xent_backward, dev, s, dloss.data_ptr(), xr.data_ptr(), w.data_ptr(),
+           tg.data_ptr(), lse.data_ptr(), *(0 if o is None else o.data_ptr() for o in outs),
+           ws.data_ptr(), n)
     return tuple(outs)
 
 
@@ -349,9 +361,8 @@ def qk_norm_rope_forward(q, k, q_weight, k_weight, positions, theta: float = 100
     qr, kr = q if q_direct else _copy(q), k if k_direct else _copy(k)
     qw, kw, pos = q_weight.contiguous(), k_weight.contiguous(), positions.contiguous()
     q_out, k_out = _empty(q), _empty(k)
-    L.apexw_qk_norm_rope_forward(s, qr.data_ptr(), kr.data_ptr(), qw.data_ptr(), kw.data_ptr(),
-                                 pos.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                                 _stream(q.device))
+    _queue(L.apexw_qk_norm_rope_forward, q.device, s, qr.data_ptr(), kr.data_ptr(),
+           qw.data_ptr(), kw.data_ptr(), pos.data_ptr(), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -370,10 +381,9 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, theta: fl
     qw, kw, pos = q_weight.contiguous(), k_weight.contiguous(), positions.contiguous()
     outs = [_empty(t) if need else None for t, need in zip((q, k, q_weight, k_weight), needs)]
     ws = _empty(ws_like)
-    L.apexw_qk_norm_rope_backward(s, dqr.data_ptr(), dkr.data_ptr(), qr.data_ptr(), kr.data_ptr(),
-                                  qw.data_ptr(), kw.data_ptr(), pos.data_ptr(),
-                                  *(0 if o is None else o.data_ptr() for o in outs),
-                                  ws.data_ptr(), n, _stream(q.device))
+    _queue(L.apexw_qk_norm_rope_backward, q.device, s, dqr.data_ptr(), dkr.data_ptr(),
+           qr.data_ptr(), kr.data_ptr(), qw.data_ptr(), kw.data_ptr(), pos.data_ptr(),
+           *(0 if o is None else o.data_ptr() for o in outs), ws.data_ptr(), n)
     return tuple(outs)
 
 
