@@ -900,6 +900,7 @@ MatArg mat(const T *p, int64_t ld, const T *p1 = nullptr) {
 // A product with epilogue EPI, split over k where that helps (slab: slab_elems).
 template <class T, bool AKS, bool BKS, int PAIR, int EPI>
 int run_split(const GemmArgs &a, float *slab, hipStream_t stream) {
+    if (a.M < 1 || a.N < 1) return APEXW_OK;           // (a grid of no blocks is refused)
     const Tiling t = pick_tiling<T>(a.M, a.N, a.K, PAIR == kPairK, true);
     if (t.splits == 1) return run_gemm<T, AKS, BKS, PAIR, EPI>(a, t, stream);
     const int64_t ld = (a.N + 31) / 32 * 32, groups = (a.e.n_store + 3) / 4;

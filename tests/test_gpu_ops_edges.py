@@ -1,0 +1,60 @@
+"""The operators at the ends of their ranges: batches without a token at real
+widths, losses whose gradient is no number, and calls from several host
+threads."""
+import threading
+
+import pytest
+import torch
+
+from tensor_adamw_optimizer_amd import _lib as L
+from tensor_adamw_optimizer_amd import ops
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _ffn(t, d, f, dtype, seed=0):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normal(*shape, std=1.0):
+        return (torch.randn(*shape, generator=gen, device=DEV) * std).to(dtype)
+
+    return (normal(t, d), normal(f, d, std=d ** -0.5), normal(f, d, std=d ** -0.5),
+            normal(d, f, std=f ** -0.5))
+
+
+# ---------------------------------------------------------- feed-forward, no tokens
+
+WIDTHS = [(64, 256), (384, 64), (1000, 2731), (1024, 4096), (4096, 1024)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,f", WIDTHS)
+def test_ffn_without_tokens(d, f, dtype):
+    """An empty batch (an expert without tokens): no output, zero gradients."""
+    x, *w = _ffn(0, d, f, dtype)
+    y, kept = ops.gated_ffn_forward(x, *w, keep=True)
+    assert y.shape == (0, d)
+    for k in (kept, None):
+        dx, *dw = ops.gated_ffn_backward(x, x, *w, kept=k)
+        assert dx.shape == (0, d)
+        for g, t in zip(dw, w):
+            assert g.shape == t.shape and not g.any()
+
+
+@pytest.mark.parametrize("dtype", [L.APEXW_BF16, L.APEXW_F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,f", WIDTHS)
+def test_ffn_without_tokens_through_the_c_abi(d, f, dtype):
+    """The same with a place for dx, which has no row to write."""
+    _, *w = _ffn(0, d, f, BF if dtype == L.APEXW_BF16 else F32)
+    shape = L.apexw_gated_ffn_shape(0, d, f, 0, 0, dtype, L.APEXW_ACT_SILU)
+    n = L.apexw_gated_ffn_workspace_bytes(shape, True, False)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=DEV)
+    dw = [torch.full_like(t, 7) for t in w]
+    dx = torch.full((d,), 7.0, device=DEV)
+    L.apexw_gated_ffn_backward(shape, 0, 0, *(t.data_ptr() for t in w), 0, 0, dx.data_ptr(),
+                               *(t.data_ptr() for t in dw), ws.data_ptr(), n,
+                               torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert (dx == 7).all() and not any(t.any() for t in dw)
