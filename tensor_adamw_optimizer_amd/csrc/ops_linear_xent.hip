@@ -101,9 +101,11 @@ __device__ __forceinline__ void put_factors(const Factors &f, int r, int t, int 
     f.row_lse[r] = f.lse[t];
     f.factor[r] = cls < 0 ? NAN : f.reduction == kNone ? f.dloss[t] : 1.0f;
 }
+// (0 where no token carries a loss: their zeros stay so if dloss is not finite)
 __device__ __forceinline__ void put_common(const Factors &f, int n) {
-    *f.common = f.reduction == kNone ? 1.0f
-                : f.reduction == kMean ? *f.dloss / (float)(n > 0 ? n : 1) : *f.dloss;
+    *f.common = n == 0 ? 0.0f
+                : f.reduction == kNone ? 1.0f
+                : f.reduction == kMean ? *f.dloss / (float)n : *f.dloss;
 }
 
 // rows_kernel, gather_kernel and factors_kernel in one launch, for at most kAtOnce
@@ -329,10 +331,12 @@ __global__ __launch_bounds__(256) void scatter_kernel(const float *slab, int64_t
         const int r = row_of[t];
         for (int n = threadIdx.x * 4; n < cols; n += 1024) {
             f32x4 s = {0, 0, 0, 0};
-            if (r >= 0)
+            if (r >= 0) {
                 for (int k = 0; k < splits; ++k)
                     s += *reinterpret_cast<const f32x4 *>(slab + k * slab_elems + r * ld + n);
-            put4(out, (int64_t)cols, t, n, cols, s * factor);
+                s *= factor;                           // (0 times a factor that is not finite: NaN)
+            }
+            put4(out, (int64_t)cols, t, n, cols, s);
         }
     }
 }

@@ -58,3 +58,44 @@ def test_ffn_without_tokens_through_the_c_abi(d, f, dtype):
                                torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert (dx == 7).all() and not any(t.any() for t in dw)
+
+
+# ---------------------------------------------------------- a loss's gradient that is no number
+
+def _xent(t, d, v, dtype, ignored, seed=0):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(t, d, generator=gen, device=DEV).to(dtype)
+    w = (torch.randn(v, d, generator=gen, device=DEV) * d ** -0.5).to(dtype)
+    target = torch.randint(0, v, (t,), generator=gen, device=DEV)
+    target[torch.randperm(t, generator=gen, device=DEV)[:int(ignored * t)]] = -100
+    return x, w, target
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("t", [5, 70, 2100])
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_ignored_tokens_under_an_overflowed_loss_scale(reduction, t, dtype, value):
+    """A row of dx whose token carries no loss is 0, whatever the loss's gradient;
+    so is everything where no token carries one."""
+    for ignored in (0.4, 1.0):
+        x, w, target = _xent(t, 72, 300, dtype, ignored)
+        off = target == -100
+        lse = ops.linear_cross_entropy_forward(x, w, target, reduction)[2]
+        dloss = torch.full((t,) if reduction == "none" else (), value, device=DEV)
+        dx, dw = ops.linear_cross_entropy_backward(x, w, target, lse, dloss, reduction)
+        assert off.any() and not dx[off].any() and not dx[off].isnan().any()
+        if ignored == 1.0:
+            assert not dw.any() and not dw.isnan().any()
+        else:
+            assert not dx[~off].isfinite().any() and not dw.isfinite().any()
+
+
+def test_an_ignored_tokens_own_gradient_is_not_looked_at():
+    x, w, target = _xent(70, 72, 300, BF, 0.3)
+    lse = ops.linear_cross_entropy_forward(x, w, target, "none")[2]
+    dloss = torch.rand(70, device=DEV)
+    want = ops.linear_cross_entropy_backward(x, w, target, lse, dloss, "none")
+    dloss[target == -100] = float("nan")
+    got = ops.linear_cross_entropy_backward(x, w, target, lse, dloss, "none")
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
