@@ -194,10 +194,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, kept: Optional[torch.Tensor]
 class _GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, activation):
-        keep = any(ctx.needs_input_grad)
-        y, kept = gated_ffn_forward(x, w_gate, w_up, w_down, activation, keep)
-        if keep:
-            ctx.save_for_backward(x, w_gate, w_up, w_down, kept)
+        y, kept = gated_ffn_forward(x, w_gate, w_up, w_down, activation, True)
+        ctx.save_for_backward(x, w_gate, w_up, w_down, kept)
         ctx.activation = activation
         return y
 
@@ -215,6 +213,11 @@ def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu") -> torch.Tensor
     x [..., D], w_gate and w_up [F, D], w_down [D, F]; ``activation`` is
     "silu" or "gelu_tanh".
     """
+    # (a function's forward sees only what requires a gradient, not whether one can
+    # be asked for: without this, evaluation would fill a kept buffer too)
+    if not torch.is_grad_enabled() or \
+            not any(t.requires_grad for t in (x, w_gate, w_up, w_down)):
+        return gated_ffn_forward(x, w_gate, w_up, w_down, activation)[0]
     return _GatedFFN.apply(x, w_gate, w_up, w_down, activation)
 
 

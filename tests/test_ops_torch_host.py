@@ -84,3 +84,25 @@ def test_the_tensors_device_is_current_for_each_call(calls, index):
         assert device == index, name
         assert args[-1] == 100 + index, name
     assert torch.cuda.current_device() == 0
+
+
+def _kept(calls):
+    """The kept buffers' places that the forward passes were given."""
+    return [args[6] for name, _, args in calls if name == "apexw_gated_ffn_forward"]
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_nothing_is_kept_where_no_backward_pass_can_follow(calls, mode):
+    """Weights of a model require gradients in evaluation and decoding too."""
+    f = [torch.nn.Parameter(t) for t in _ffn("cuda:0")]
+    with mode():
+        assert not ops.gated_ffn(*f).requires_grad
+    assert not ops.gated_ffn(*(t.detach() for t in f)).requires_grad
+    assert _kept(calls) == [0, 0]
+
+
+@pytest.mark.parametrize("i", range(4))
+def test_the_buffer_is_kept_where_a_gradient_is_asked_for(calls, i):
+    f = _ffn("cuda:0")
+    f[i].requires_grad_()
+    assert ops.gated_ffn(*f).requires_grad and _kept(calls) == [1 << 20]
