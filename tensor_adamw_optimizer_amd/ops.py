@@ -177,16 +177,20 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, kept: Optional[torch.Tensor]
     false) for the gradient ``dy`` of the output."""
     if dy.shape != x.shape:
         raise ValueError("gated_ffn: dy is %s, x %s" % (tuple(dy.shape), tuple(x.shape)))
-    s, direct, dy_direct, _, _, n, ws_like = _plan(
+    s, direct, dy_direct, kept_len, _, n, ws_like = _plan(
         _ffn_plan, _sig(x), _sig(w_gate), _sig(w_up), _sig(w_down), _sig(dy), activation,
         kept is not None, _aligned(x), _aligned(dy))
+    if kept is not None and (kept.dtype != torch.uint8 or kept.device != x.device or
+                             kept.shape != (kept_len,) or not kept.is_contiguous()):
+        raise ValueError("gated_ffn: kept must be the buffer of the forward pass over the same "
+                         "inputs, %d contiguous bytes (uint8) on %s" % (kept_len, x.device))
     w_gate, w_up, w_down = _whole(w_gate), _whole(w_up), _whole(w_down)
     xr, dyr = x if direct else _copy(x), dy if dy_direct else _copy(dy)
     outs = [_empty(t) if need else None for t, need in zip((x, w_gate, w_up, w_down), needs)]
     ws = _empty(ws_like)
     _queue(L.apexw_gated_ffn_backward, x.device, s, dyr.data_ptr(), xr.data_ptr(),
            w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
-           0 if kept is None else kept.data_ptr(), 0 if kept is None else kept.numel(),
+           0 if kept is None else kept.data_ptr(), kept_len,
            *(0 if o is None else o.data_ptr() for o in outs), ws.data_ptr(), n)
     return tuple(outs)
 

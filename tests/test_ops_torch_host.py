@@ -106,3 +106,23 @@ def test_the_buffer_is_kept_where_a_gradient_is_asked_for(calls, i):
     f = _ffn("cuda:0")
     f[i].requires_grad_()
     assert ops.gated_ffn(*f).requires_grad and _kept(calls) == [1 << 20]
+
+
+def test_a_kept_buffer_that_is_not_the_forward_passs_is_refused(calls):
+    """Its address goes to the GPU as it is: a host tensor's would be read there."""
+    f = _ffn("cuda:0")
+    _, kept = ops.gated_ffn_forward(*f, keep=True)
+    n = kept.numel()
+    wrong = (torch.empty(n, dtype=torch.uint8),                            # on the host
+             torch.empty(n, dtype=torch.uint8, device="cuda:1"),
+             torch.empty(n, dtype=torch.float32, device="cuda:0"),
+             torch.empty(n - 256, dtype=torch.uint8, device="cuda:0"),
+             torch.empty(n + 256, dtype=torch.uint8, device="cuda:0"),     # of more tokens
+             torch.empty(2 * n, dtype=torch.uint8, device="cuda:0")[::2])
+    made = len(calls)
+    for k in wrong:
+        with pytest.raises(ValueError, match="kept"):
+            ops.gated_ffn_backward(f[0], *f, kept=k)
+    assert len(calls) == made
+    ops.gated_ffn_backward(f[0], *f, kept=kept)
+    assert calls[-1][0] == "apexw_gated_ffn_backward" and calls[-1][2][6:8] == (1 << 20, n)
