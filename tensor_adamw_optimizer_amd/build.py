@@ -18,7 +18,7 @@ OP_SRCS = [os.path.join(CSRC, n) for n in ("ops_gated_ffn.hip", "ops_linear_xent
                                                "ops_qk_norm_rope.hip")]
 DEPS = [SRC, *OP_SRCS, os.path.join(ROOT, "include", "apexw.h"),
         *(os.path.join(CSRC, n) for n in ("apexw_kernels.hpp", "apexw_plan.hpp", "ops_common.hpp",
-                                          "ops_gemm.hpp", "ops_rows.hpp"))]
+                                          "ops_gemm.hpp", "ops_rounds.hpp", "ops_rows.hpp"))]
 LIB = os.path.join(HERE, "libapexw.so")
 ARCH = os.environ.get("APEXW_OFFLOAD_ARCH", "gfx950")
 

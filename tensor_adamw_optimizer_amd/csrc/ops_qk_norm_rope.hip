@@ -23,6 +23,7 @@
 // next row's values under way the backward pass 122; of 3 to 6 waves a unit's
 // fourth, 4 measured best (6 spill: 288 us for both).
 #include "ops_common.hpp"
+#include "ops_rounds.hpp"
 
 // Multiply-adds are written out: what the values are reached by (Mode) does not
 // change a bit.
@@ -235,7 +236,8 @@ __global__ __launch_bounds__(kThreads, 4) void forward_kernel(const QkArgs a) {
     const float inv = 1.0f / a.head_dim;
     const int at = threadIdx.x / G, pq = gridDim.y == 1 ? 1 : passes(a.q_heads, R);
     int set = 0;
-    for (int t0 = blockIdx.x * TPI; t0 < a.tokens; t0 += gridDim.x * TPI, set ^= 1) {
+    for (int t0 = blockIdx.x * TPI; t0 < a.tokens;
+         t0 = next_round(t0, gridDim.x * TPI, a.tokens), set ^= 1) {
         angles.round(a, set, t0);
         const int left = a.tokens - t0 < TPI ? a.tokens - t0 : TPI;
         auto rows = [&](const Heads &in, const void *weight, void *out, Rows r) {
@@ -286,7 +288,8 @@ __global__ __launch_bounds__(kThreads, MODE == kSingle ? 2 : 4) void backward_ke
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum_q[j] = sum_k[j] = 0.0f;
     int set = 0;
-    for (int t0 = blockIdx.x * TPI; t0 < a.tokens; t0 += gridDim.x * TPI, set ^= 1) {
+    for (int t0 = blockIdx.x * TPI; t0 < a.tokens;
+         t0 = next_round(t0, gridDim.x * TPI, a.tokens), set ^= 1) {
         angles.round(a, set, t0);
         const int left = a.tokens - t0 < TPI ? a.tokens - t0 : TPI;
         auto rows = [&](const Heads &in, const Heads &gr, const void *weight, void *out,
