@@ -502,7 +502,7 @@ __device__ __forceinline__ void epilogue(f32x4 (&acc)[FM][FN], char *lds, const 
         if constexpr (EPI == kEpiLse) {
             static_assert(PASS * 16 <= 64, "a lane a row");
             const int m = m0 + P0 * 16 + lane;
-            if (lane < PASS * 16 && m < M) reduce_row<WC>(lds, e, lane, m, n0, N, e.target[m]);
+            if (lane < PASS * 16 && m < M) reduce_row<WC>(lds, e, lane, m, n0, N, e.target[m] - e.col0);
         } else if (inside) {
             rows(Int<0>());
         } else {

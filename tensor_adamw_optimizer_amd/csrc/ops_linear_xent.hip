@@ -10,7 +10,8 @@
 //
 // Forward: one product whose epilogue reduces each 32 or 64 columns of a row to
 // their largest logit and the sum of exp(z - largest); a second kernel joins
-// these pairs.  Backward, in pieces of the vocabulary: p of a piece from a
+// these pairs.  More than 2^30 logits are formed in pieces of the vocabulary, the
+// pairs of a piece joined to those before it.  Backward, in pieces of the vocabulary: p of a piece from a
 // second product over x and W, then the piece's rows of dW, and the piece's
 // share of dx added to an fp32 array.  Forming z twice costs a quarter of the
 // pass (8 instead of 6 T D V); the logits would take 4 T V bytes.
@@ -163,14 +164,14 @@ __device__ __forceinline__ void join(float &top, float &sum, float2 p) {
 // A row's pair and its target's logit from slabs of a product split over k (small
 // vocabularies, whose tiles alone would not fill the chip): a workgroup a row.
 __global__ __launch_bounds__(256) void reduce_slabs_kernel(const float *slab, int64_t slab_elems,
-                                                           int splits, int64_t ld, int32_t cols,
-                                                           const int32_t *count,
+                                                           int splits, int64_t ld, int32_t col0,
+                                                           int32_t cols, const int32_t *count,
                                                            const int32_t *class_of, float2 *part,
                                                            float *z_target) {
     __shared__ float2 lds[256];
     const int r = blockIdx.x;
     if (r >= *count) return;
-    const int t = class_of[r];
+    const int t = class_of[r] - col0;
     float top = -INFINITY, sum = 0.0f;
     for (int n = threadIdx.x * 4; n < cols; n += 1024) {
         f32x4 v = {0, 0, 0, 0};
@@ -194,8 +195,10 @@ __global__ __launch_bounds__(256) void reduce_slabs_kernel(const float *slab, in
     if (threadIdx.x == 0) part[r] = make_float2(top, sum);
 }
 
-// Joins each row's pairs: 16 rows a workgroup, 16 threads a row.
+// Joins each row's pairs, in pieces of the vocabulary to that of the pieces before:
+// 16 rows a workgroup, 16 threads a row.  The last piece has the row's results.
 __global__ __launch_bounds__(256) void join_kernel(const float2 *part, int64_t ld, int32_t groups,
+                                                   float2 *before, bool first, bool last,
                                                    const int32_t *count, const int32_t *token_of,
                                                    const int32_t *class_of, const float *z_target,
                                                    float *token_loss, float *lse) {
@@ -212,6 +215,11 @@ __global__ __launch_bounds__(256) void join_kernel(const float2 *part, int64_t l
     __syncthreads();
     if (k != 0 || r >= rows) return;
     for (int j = 1; j < 16; ++j) join(top, sum, lds[threadIdx.x + 16 * j]);
+    if (!first) join(top, sum, before[r]);
+    if (!last) {
+        before[r] = make_float2(top, sum);
+        return;
+    }
     const float l = top + logf(sum);
     const int t = token_of[r];
     lse[t] = l;
@@ -355,11 +363,15 @@ struct Xent {
     // workspace
     int32_t *count, *token_of, *class_of, *row_of;
     T *xc, *wp, *p;
-    float *part, *z_target, *row_lse, *factor, *common, *slab, *dw_slab;
+    float *part, *before, *z_target, *row_lse, *factor, *common, *slab, *dw_slab;
 
     bool pad_d() const { return s.D % (16 / sizeof(T)) != 0; }
 
-    // Classes in a piece: p stays within 256 MiB, and a piece is whole tiles.
+    // Classes in a piece of the backward pass: whole tiles, and p within 256 MiB, up
+    // to 2^16 tokens in bf16 and 2^15 in fp32.  Of more tokens p has 2048 classes all
+    // the same, 4 GiB of 2^20 in bf16: each piece reads and writes dx's fp32 sums, 8
+    // bytes a token and width, half the time of such a piece's product; of narrower
+    // pieces, four times it at 256 classes.
     int64_t piece() const {
         const int64_t c = ((int64_t)1 << 28) / ((s.T > 0 ? s.T : 1) * (int64_t)sizeof(T)) / 2048 * 2048;
         return c < 2048 ? (s.V < 2048 ? s.V : 2048) : c < s.V ? c : s.V;
@@ -411,12 +423,21 @@ struct Xent {
         return a;
     }
 
+    // Classes in a piece of the forward pass: whole tiles, and at most 2^30 logits, so
+    // that their pairs stay within some 256 MiB and a launch's threads far below 2^32.
+    int64_t forward_piece() const {
+        const int64_t most = ((int64_t)1 << 30) / (s.T > 0 ? s.T : 1) / 256 * 256;
+        if (s.V <= most) return s.V;
+        return div_up(div_up(s.V, div_up(s.V, most)), 256) * 256;
+    }
+    int64_t forward_last() const { return s.V - (s.V - 1) / forward_piece() * forward_piece(); }
+
     Tiling tiling(int64_t classes) const { return pick_tiling<T>(s.T, classes, s.D, false, true); }
     // Groups of columns that are reduced to a pair, those of the last tile's
-    // columns past the vocabulary too.
-    int64_t groups() const {
-        const Tiling t = tiling(s.V);
-        return t.splits > 1 ? 1 : div_up(s.V, t.bn) * (t.bn / t.wave_cols);
+    // columns past the piece too.
+    int64_t groups(int64_t classes) const {
+        const Tiling t = tiling(classes);
+        return t.splits > 1 ? 1 : div_up(classes, t.bn) * (t.bn / t.wave_cols);
     }
 
     // A few tokens: all of them go through the product, where it lies in memory.
@@ -426,10 +447,18 @@ struct Xent {
     bool at_once() const { return few_groups() * s.T <= 32768; }
 
     int64_t place_forward(Bump &b) {
-        if (!few()) place_rows(b);
-        part = b.take<float>((few() ? few_groups() : groups()) * s.T * 2);
+        if (few()) {
+            part = b.take<float>(few_groups() * s.T * 2);
+            z_target = b.take<float>(s.T);
+            return b.used;
+        }
+        place_rows(b);
+        const int64_t c = forward_piece(), last = forward_last();
+        part = b.take<float>((groups(c) > groups(last) ? groups(c) : groups(last)) * s.T * 2);
+        before = b.take<float>(c < s.V ? s.T * 2 : 0);
         z_target = b.take<float>(s.T);
-        slab = b.take<float>(few() ? 0 : slab_elems<T>(s.T, s.V, s.D));
+        const int64_t n0 = slab_elems<T>(s.T, c, s.D), n1 = slab_elems<T>(s.T, last, s.D);
+        slab = b.take<float>(n0 > n1 ? n0 : n1);
         return b.used;
     }
 
@@ -462,29 +491,34 @@ struct Xent {
     int forward(float *loss, float *token_loss, float *lse) {
         if (few()) return few_forward(loss, token_loss, lse);
         APEXW_TRY(rows(Factors{}));
-        GemmArgs a = logits(0, s.V);
-        const Tiling t = tiling(s.V);
-        if (t.splits == 1) {
-            a.e.f0 = part;
-            a.e.f1 = z_target;
-            a.e.ld = s.T;
-            APEXW_TRY((run_gemm<T, false, false, kPairNone, kEpiLse>(a, t, stream)));
-        } else {
-            const int64_t ld = (s.V + 31) / 32 * 32;
-            a.e.f0 = slab;
-            a.e.ld = ld;
-            a.e.slab = s.T * ld;
-            a.e.n_store = (int)ld;
-            APEXW_TRY((run_gemm<T, false, false, kPairNone, kEpiSlab>(a, t, stream)));
-            reduce_slabs_kernel<<<(int)s.T, 256, 0, stream>>>(slab, s.T * ld, t.splits, ld, (int)s.V,
-                                                              count, class_of, (float2 *)part,
-                                                              z_target);
+        const int64_t c = forward_piece();
+        for (int64_t c0 = 0; c0 < s.V; c0 += c) {
+            const int64_t n = s.V - c0 < c ? s.V - c0 : c;
+            GemmArgs a = logits(c0, n);
+            const Tiling t = tiling(n);
+            if (t.splits == 1) {
+                a.e.f0 = part;
+                a.e.f1 = z_target;
+                a.e.ld = s.T;
+                a.e.col0 = (int)c0;
+                APEXW_TRY((run_gemm<T, false, false, kPairNone, kEpiLse>(a, t, stream)));
+            } else {
+                const int64_t ld = (n + 31) / 32 * 32;
+                a.e.f0 = slab;
+                a.e.ld = ld;
+                a.e.slab = s.T * ld;
+                a.e.n_store = (int)ld;
+                APEXW_TRY((run_gemm<T, false, false, kPairNone, kEpiSlab>(a, t, stream)));
+                reduce_slabs_kernel<<<(int)s.T, 256, 0, stream>>>(slab, s.T * ld, t.splits, ld,
+                                                                  (int)c0, (int)n, count, class_of,
+                                                                  (float2 *)part, z_target);
+                APEXW_TRY_HIP(hipGetLastError());
+            }
+            join_kernel<<<(int)div_up(s.T, 16), 256, 0, stream>>>(
+                (const float2 *)part, s.T, (int)groups(n), (float2 *)before, c0 == 0, c0 + n == s.V,
+                count, token_of, class_of, z_target, token_loss, lse);
             APEXW_TRY_HIP(hipGetLastError());
         }
-        join_kernel<<<(int)div_up(s.T, 16), 256, 0, stream>>>(
-            (const float2 *)part, s.T, (int)groups(), count, token_of, class_of, z_target, token_loss,
-            lse);
-        APEXW_TRY_HIP(hipGetLastError());
         reduce_kernel<<<1, 1024, 0, stream>>>(row_of, count, (int)s.T, s.reduction, token_loss, lse,
                                               loss);
         APEXW_TRY_HIP(hipGetLastError());
