@@ -130,14 +130,19 @@ __device__ __forceinline__ void mma_in_place(const Frag &n, const Frag &m, f32x4
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(n.v), "v"(m.v));
 }
 
-// Stands between mma_in_place and other uses of the accumulators, either way.
+// Stands between mma_in_place and other uses of the accumulators, either way: all
+// that writes them comes before the wait, all that reads them after it.
 template <int M, int N>
 __device__ __forceinline__ void settle(f32x4 (&acc)[M][N]) {
+    auto hold = [&] {
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+    hold();
     asm volatile("s_nop 15" ::);
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j) asm volatile("" : "+a"(acc[i][j]));
+    hold();
 }
 
 // ---- the operand's way through LDS
@@ -210,11 +215,10 @@ __device__ __forceinline__ Frag load_frag(const char *tile, int row, int s, int 
 // output register and is waited for by count, by hand: the compiler does not
 // track it.  No memory clobber: reads of LDS may move over it, since between two
 // barriers nobody reads the buffer that it fills; `arrive` is what orders them.
-// (M0, which it writes, is a register that the compiler keeps nothing in.)
 template <int AT>
 __device__ __forceinline__ void lds_load(uint32_t lds, uint32_t off, i32x4 rsrc) {
     asm volatile("s_add_i32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(rsrc), "n"(AT) : "scc");
+                 :: "s"(lds), "v"(off), "s"(rsrc), "n"(AT) : "m0", "scc");
 }
 
 // All but the last N direct loads have landed and all reads of LDS are done,
