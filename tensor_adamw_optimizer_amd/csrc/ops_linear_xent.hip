@@ -440,8 +440,17 @@ struct Xent {
         return t.splits > 1 ? 1 : div_up(classes, t.bn) * (t.bn / t.wave_cols);
     }
 
-    // A few tokens: all of them go through the product, where it lies in memory.
-    bool few() const { return s.T <= kRowsMax; }
+    // A few tokens: all of them go through the product of ops_rows.hpp, which reads
+    // the weight where it lies.  More than 32 with a large weight: the tiles fetch that
+    // faster, unless it would have to be copied to padded rows first.  Measured, us,
+    // rows against tiles: 24 tokens, bf16, 2048 x 32000 37 and 49, 4096 x 131072 249
+    // and 233, fp32 506 and 569; 48 tokens, bf16, 1024 x 32000 (63 MiB) 34 and 40,
+    // 2048 x 32000 53 and 49, 4096 x 131072 346 and 235, 1030 x 32000 (padded) 32
+    // and 74; 64 tokens, fp32, 512 x 32000 43 and 50, 4096 x 32000 225 and 173.
+    bool few() const {
+        return s.T <= 32 || (s.T <= kRowsMax && (s.V * s.D * (int64_t)sizeof(T) <= (int64_t)64 << 20 ||
+                                                 pad_d()));
+    }
     RowsTiling few_tiling() const { return rows_tiling(s.V, 1); }
     int64_t few_groups() const { return div_up(s.V, few_tiling().nf * 16); }
     bool at_once() const { return few_groups() * s.T <= 32768; }

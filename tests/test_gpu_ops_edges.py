@@ -138,3 +138,14 @@ def test_xent_forward_of_very_many_tokens_and_classes():
     x, w, target = _xent(t, 8, v, BF, 0.0, seed=9)
     got = ops.linear_cross_entropy_forward(x, w, target)
     _scored(x, w, target, torch.tensor([0, 1, 77777, t - 2, t - 1], device=DEV), got)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("t", [32, 33, 64, 65])
+@pytest.mark.parametrize("d,v", [(2048, 16411), (2050, 16411), (72, 16411)])
+def test_xent_on_both_sides_of_a_few_tokens(t, d, v, dtype):
+    """Weights large and small, and one whose rows the tiles would have padded."""
+    x, w, target = _xent(t, d, v, dtype, 0.2, seed=t)
+    target[3] = v - 1
+    got = ops.linear_cross_entropy_forward(x, w, target)
+    _scored(x, w, target, torch.arange(t, device=DEV), got)
