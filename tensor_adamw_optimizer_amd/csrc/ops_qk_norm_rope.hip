@@ -399,7 +399,7 @@ struct Shape {
 
 int lanes(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : head_dim <= 256 ? 32 : 64; }
 
-int check_shape(const apexw_qk_norm_rope_shape *p, Shape &s) {
+int check_shape(const apexw_qk_norm_rope_shape *p, bool backward, Shape &s) {
     if (p == nullptr) return fail(APEXW_EINVAL, "shape is NULL");
     if (p->dtype != APEXW_F32 && p->dtype != APEXW_BF16)
         return fail(APEXW_EDTYPE, "unknown element type %d", p->dtype);
@@ -424,9 +424,13 @@ int check_shape(const apexw_qk_norm_rope_shape *p, Shape &s) {
     s.rows = kThreads / lanes(p->head_dim);
     // Few tokens: a token a round, and a workgroup for each pass over its heads.
     // Many: rounds of four tokens with all of their heads, workgroups walking
-    // over them.
+    // over them.  Measured, us, few against many, 32 + 8 heads of 128, bf16: forward
+    // 256 tokens 4.2 and 8.0, 768 7.1 and 8.7, 1024 8.5 and 9.1, 1536 11.1 and 9.8;
+    // backward, whose workgroups leave a row of sums each, 256 tokens 10.6 and 13.1,
+    // 512 14.8 and 13.8, 1024 23.5 and 15.1.  12 + 3 heads of 96 and fp32 meet at the
+    // same numbers of tokens.
     const int passes = (int)(div_up(p->q_heads, s.rows) + div_up(p->k_heads, s.rows));
-    s.many = p->tokens >= 1024;
+    s.many = p->tokens >= (backward ? 512 : 1024);
     s.gx = !s.many ? (int)p->tokens : (int)(div_up(p->tokens, kTokens) < 1024 ? div_up(p->tokens, kTokens) : 1024);
     s.gy = s.many ? 1 : passes;
     return APEXW_OK;
@@ -525,7 +529,7 @@ extern "C" int apexw_qk_norm_rope_forward(const apexw_qk_norm_rope_shape *shape,
                                           const void *k_weight, const int64_t *positions,
                                           void *q_out, void *k_out, void *stream) {
     Shape s;
-    APEXW_TRY(check_shape(shape, s));
+    APEXW_TRY(check_shape(shape, false, s));
     if (s.p.tokens == 0) return APEXW_OK;
     const void *const ptrs[6] = {q, k, q_weight, k_weight, q_out, k_out};
     const char *const names[6] = {"q", "k", "q_weight", "k_weight", "q_out", "k_out"};
@@ -540,7 +544,7 @@ extern "C" int apexw_qk_norm_rope_forward(const apexw_qk_norm_rope_shape *shape,
 extern "C" int apexw_qk_norm_rope_workspace_bytes(const apexw_qk_norm_rope_shape *shape,
                                                   size_t *out_bytes) {
     Shape s;
-    APEXW_TRY(check_shape(shape, s));
+    APEXW_TRY(check_shape(shape, true, s));
     if (out_bytes == nullptr) return fail(APEXW_EINVAL, "out_bytes is NULL");
     *out_bytes = (size_t)work_bytes(s);
     return APEXW_OK;
@@ -553,7 +557,7 @@ extern "C" int apexw_qk_norm_rope_backward(const apexw_qk_norm_rope_shape *shape
                                            void *dq_weight, void *dk_weight, void *workspace,
                                            size_t workspace_len, void *stream) {
     Shape s;
-    APEXW_TRY(check_shape(shape, s));
+    APEXW_TRY(check_shape(shape, true, s));
     const void *const ptrs[10] = {dq, dk, q, k, q_weight, k_weight, q_grad, k_grad, dq_weight, dk_weight};
     const char *const names[10] = {"dq", "dk", "q", "k", "q_weight", "k_weight", "q_grad", "k_grad",
                                    "dq_weight", "dk_weight"};

@@ -149,3 +149,22 @@ def test_xent_on_both_sides_of_a_few_tokens(t, d, v, dtype):
     target[3] = v - 1
     got = ops.linear_cross_entropy_forward(x, w, target)
     _scored(x, w, target, torch.arange(t, device=DEV), got)
+
+
+# ---------------------------------------------------------- norm with rotation, grids of few and many tokens
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("t", [511, 512, 1023, 1024, 1025])
+@pytest.mark.parametrize("hq,hk,hd,rotary", [(12, 3, 96, 48), (5, 2, 33, 16)])
+def test_qk_on_both_sides_of_many_tokens(t, hq, hk, hd, rotary, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(t)
+    q, k, dq, dk = (torch.randn(t, h, hd, generator=gen, device=DEV).to(dtype) for h in (hq, hk, hq, hk))
+    qw, kw = (torch.rand(hd, generator=gen, device=DEV).to(dtype) + 0.5 for _ in range(2))
+    pos = torch.randint(0, 5000, (t,), generator=gen, device=DEV)
+    got = [*ops.qk_norm_rope_forward(q, k, qw, kw, pos, rotary_dim=rotary),
+           *ops.qk_norm_rope_backward(dq, dk, q, k, qw, kw, pos, rotary_dim=rotary)]
+    a = R.qk(q, qw, pos, dtype, rotary=rotary, dy=dq)
+    b = R.qk(k, kw, pos, dtype, rotary=rotary, dy=dk)
+    for name, x, (want, bound) in zip(("q", "k", "dq", "dk", "dqw", "dkw"), got,
+                                      (a[0], b[0], a[1], b[1], a[2], b[2])):
+        R.within(x, want, bound, name)
