@@ -1,6 +1,6 @@
 """The operators at the ends of their ranges: batches without a token at real
-widths, losses whose gradient is no number, and calls from several host
-threads."""
+widths, losses whose gradient is no number, more logits than one launch forms, both
+sides of the rules that choose a kernel, and calls from several host threads."""
 import threading
 
 import pytest
@@ -168,3 +168,44 @@ def test_qk_on_both_sides_of_many_tokens(t, hq, hk, hd, rotary, dtype):
     for name, x, (want, bound) in zip(("q", "k", "dq", "dk", "dqw", "dkw"), got,
                                       (a[0], b[0], a[1], b[1], a[2], b[2])):
         R.within(x, want, bound, name)
+
+
+# ---------------------------------------------------------- host threads
+
+def test_two_host_threads_on_two_streams():
+    """Shapes and streams of their own, the same plans and tile choices met from
+    both sides: each thread's results are those of one thread alone."""
+    def work(seed):
+        out = []
+        for i in range(12):
+            t, d, f = 1 + 37 * i, 64 + 8 * i, 96 + 16 * (i % 5)
+            x, *w = _ffn(t, d, f, (BF, F32)[i % 2], seed=seed + i)
+            y, kept = ops.gated_ffn_forward(x, *w, keep=True)
+            out += [y, *ops.gated_ffn_backward(x, x, *w, kept=kept)]
+            x, w, target = _xent(t, d, 100 + 301 * i, (BF, F32)[i % 2], 0.2, seed=seed + i)
+            a = ops.linear_cross_entropy_forward(x, w, target)
+            out += [*a, *ops.linear_cross_entropy_backward(x, w, target, a[2], a[0])]
+        return out
+
+    alone = [work(0), work(100)]
+    got, wrong = [None, None], []
+
+    def run(n):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(3):
+                    got[n] = work(100 * n)
+            stream.synchronize()
+        except Exception as e:                              # noqa: BLE001
+            wrong.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(n,)) for n in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
