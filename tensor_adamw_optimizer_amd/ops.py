@@ -123,9 +123,17 @@ def _empty(like: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
+_elements: dict = {}
+
+
 def _like(dtype, device, *shape) -> torch.Tensor:
-    """What _empty makes tensors of that shape from: one element, expanded."""
-    return torch.empty((), dtype=dtype, device=device).expand(shape)
+    """What _empty makes tensors of that shape from: one element, expanded, the same
+    one for all plans (one of a plan's own, made under graph capture, would hold on
+    to the graph's memory)."""
+    e = _elements.get((dtype, device))
+    if e is None:
+        e = _elements[dtype, device] = torch.empty((), dtype=dtype, device=device)
+    return e.expand(shape)
 
 
 # ------------------------------------------------------ gated feed-forward

@@ -209,3 +209,47 @@ def test_two_host_threads_on_two_streams():
     assert not wrong, wrong
     for a, b in zip(alone, got):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ---------------------------------------------------------- graphs
+
+def test_a_released_graph_leaves_no_memory_behind():
+    """Shapes first seen under capture, too: what is kept of a call's plan is not in
+    the graph's memory, which would then stay for as long as the plan does."""
+    def calls(t):
+        x, *w = _ffn(t, 64, 96, BF)
+        y, kept = ops.gated_ffn_forward(x, *w, keep=True)
+        ops.gated_ffn_backward(x, x, *w, kept=kept)
+        x, w, target = _xent(t, 64, 300, BF, 0.0)
+        lse = ops.linear_cross_entropy_forward(x, w, target)[2]
+        ops.linear_cross_entropy_backward(x, w, target, lse, torch.ones((), device=DEV))
+        q, pos = x.view(t, 2, 32), target
+        ops.qk_norm_rope_backward(q, q, q, q, w[0, :32], w[0, :32], pos)
+
+    def captured(t):
+        x, *w = _ffn(t, 64, 96, BF)
+        xe, we, target = _xent(t, 64, 300, BF, 0.0)
+        one = torch.ones((), device=DEV)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y, kept = ops.gated_ffn_forward(x, *w, keep=True)
+            g = ops.gated_ffn_backward(x, x, *w, kept=kept)
+            lse = ops.linear_cross_entropy_forward(xe, we, target)[2]
+            h = ops.linear_cross_entropy_backward(xe, we, target, lse, one)
+            r = ops.qk_norm_rope_backward(*[xe.view(t, 2, 32)] * 4, we[0, :32], we[0, :32], target)
+        graph.replay()
+        torch.cuda.synchronize()
+        del y, kept, g, lse, h, r
+        graph.reset()
+
+    def held():
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        return torch.cuda.memory_reserved()
+
+    calls(7)
+    captured(7)
+    before = held()
+    for t in (70, 71, 72):
+        captured(t)
+    assert held() == before

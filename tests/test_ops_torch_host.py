@@ -40,6 +40,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(ops, "_raw_stream", lambda index: 100 + index)
     monkeypatch.setattr(torch.Tensor, "data_ptr", lambda t: 1 << 20)
     monkeypatch.setattr(ops, "_plans", {})
+    monkeypatch.setattr(ops, "_elements", {})
     with FakeTensorMode():
         yield made
 
