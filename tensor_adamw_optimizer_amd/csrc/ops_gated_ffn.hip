@@ -16,7 +16,7 @@
 // bf16 copies.  All sums are fp32.
 //
 // Measured on an MI355X, bf16: 8192 tokens, 4096 x 14336, forward and backward
-// 6.8 ms (1280 TFLOP/s; the products' rate, 1.3 to 1.4 PFLOP/s, and 0.4 ms for the
+// 6.7 ms (1285 TFLOP/s; the products' rate, 1.3 to 1.4 PFLOP/s, and 0.4 ms for the
 // kept fp32 values' 2.3 GB); 512 tokens, 1024 x 2816, 75 us in six launches, bound
 // by each launch's fill and drain; one token, 4096 x 14336, forward 65 us (5.4
 // TB/s of weights).

@@ -23,7 +23,7 @@
 // over the pieces are fp32, the mean's sum is fp64.
 //
 // Measured on an MI355X, bf16: 8192 tokens, 4096 x 131072, forward and backward
-// 26.3 ms (1340 TFLOP/s of the 8 T D V, the products' rate); 4096 tokens, a quarter
+// 26.2 ms (1340 TFLOP/s of the 8 T D V, the products' rate); 4096 tokens, a quarter
 // of them without a loss, 2048 x 49999, 2.3 ms; 16 tokens scored, 2048 x 32000, 33
 // us (26 us of it the weight's 131 MB).
 #include "ops_rows.hpp"

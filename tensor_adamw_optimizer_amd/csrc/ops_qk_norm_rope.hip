@@ -17,11 +17,13 @@
 // gradients are summed in registers over a workgroup's tokens and heads, then
 // over workgroups in a fixed order by a second launch: no atomics.
 //
-// Bound by memory: 16384 tokens, 32 + 8 heads of 128, bf16, forward 61 us (5.5
-// TB/s) and backward 105 us (4.8 TB/s) on an MI355X; 32 tokens 3.6 us.  With the
-// angles formed by every lane for itself the two took 91 and 146 us, without the
-// next row's values under way the backward pass 122; of 3 to 6 waves a unit's
-// fourth, 4 measured best (6 spill: 288 us for both).
+// Bound by memory: 16384 tokens, 32 + 8 heads of 128, bf16, forward 69 us (4.9
+// TB/s) and backward 103 us (4.9 TB/s) on an MI355X, fp32 131 (5.1) and 203 (5.0);
+// 32 tokens 3.6 us.  With the angles formed by every lane for itself the two took
+// 91 and 146 us, without the next row's values under way the backward pass 122; of
+// 3 to 6 waves a unit's fourth, 4 measured best in bf16 (6 spill: 288 us for both).
+// In fp32 four waves leave the backward pass's vector modes two or four registers
+// short, which pass through 12 or 20 bytes of scratch memory a lane.
 #include "ops_common.hpp"
 #include "ops_rounds.hpp"
 

@@ -11,8 +11,10 @@
 // happens to the result is the same as under ops_gemm.hpp.
 //
 // Measured on an MI355X, bf16: one row, 28672 x 4096 42 us (5.6 TB/s), 4096 x 14336
-// 22 us (5.3 TB/s); 16 rows, 32000 x 2048 26 us (5.0 TB/s).  With branches around
-// the loads the compiler waits for all of them at once: 51, 30 and 31 us.
+// 22 us (5.3 TB/s); 16 rows, 32000 x 2048 26 us (5.0 TB/s, with the matrix's 131 MB
+// in the 256 MB Infinity Cache from the call before; eight such matrices in turn take
+// 3 us more a call).  With branches around the loads the compiler waits for all of
+// them at once: 51, 30 and 31 us.
 //
 // Rows need no padding: a 16-byte load is made at any element's alignment, and
 // the end of a row that is no whole step is read value by value.
